@@ -83,9 +83,11 @@ cudaError_t launch_decode(const DecodeArgs& a, bool e4m3, cudaStream_t stream) {
   const int tiles = decode_tiles(p.group), rows = 8 * tiles;
   p.runs = (p.group + rows - 1) / rows;
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  p.cap = a.softcap * 1.4426950408889634f;
-  // the scores come in units of log2, tanh takes s / cap
-  p.inv_cap = a.softcap > 0.f ? 0.6931471805599453f / a.softcap : 0.f;
+  // the scores come in units of log2, tanh takes s / cap; a cap at either end
+  // of fp32 counts as the nearest whose product and quotient are finite
+  const float cap = fminf(fmaxf(a.softcap, FLT_MIN), 0x1p127f);
+  p.cap = cap * 1.4426950408889634f;
+  p.inv_cap = 0.6931471805599453f / cap;
   p.desc = static_cast<JoinDesc*>(a.workspace);
   p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) +
                                      decode_desc_bytes(tiles));
