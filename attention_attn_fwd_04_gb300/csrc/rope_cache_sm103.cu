@@ -233,7 +233,10 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* y) {
 template <int W>
 __device__ __forceinline__ void store_item_e4m3(uint8_t* row, const Item<W>& it, float* y,
                                                 float scale) {
-  const float inv = fminf(__fdiv_rn(1.0f, scale), FLT_MAX);  // 0 stays 0 for any scale
+  // 0 stays 0 for a scale of 0 or one whose reciprocal is beyond fp32, and every
+  // number becomes 0 for an infinite one, as the quotient does
+  const float inv = fminf(__fdiv_rn(1.0f, scale), FLT_MAX);
+  if (inv == 0.0f) scale = 0.0f;  // the remainder times infinity would be NaN
 #pragma unroll
   for (int i = 0; i < 2 * W; ++i) y[i] = scaled(y[i], scale, inv);
   store_e4m3<W>(row + it.a, y);
