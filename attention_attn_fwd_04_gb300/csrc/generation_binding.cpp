@@ -111,6 +111,13 @@ T* data(const at::Tensor& t) {
   return static_cast<T*>(t.data_ptr());
 }
 
+// After a call that writes into a caller's tensor: its next version, so that
+// autograd's check of the tensors it saved sees the write.  Tensors of inference
+// mode have no version.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 const attn_rope_plan* plan_at(PyObject* o) {
   const unsigned long long a = PyLong_AsUnsignedLongLong(o);
   if (a == (unsigned long long)-1 && PyErr_Occurred()) throw Refused();
@@ -172,6 +179,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
           x.data_ptr(), strides(x), y.data_ptr(), strides(y), narrow(B, "B"), narrow(H, "H"),
           narrow(S, "S"), narrow(D, "D"), pos, pos_stride, offset, plan, stream_of(dev));
       if (st != ATTN_OK) return PyLong_FromLong(st);
+      if (given(a[5])) written(y);
     }
     return THPVariable_Wrap(std::move(y));
   });
@@ -238,7 +246,9 @@ PyObject* slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
         data<int32_t>(out[3]), data<int64_t>(out[4]), pool ? data<int32_t>(out[5]) : nullptr, T,
         stream_of(dev));
     if (st != ATTN_OK) return PyLong_FromLong(st);
+    if (pool) written(table);
     if (given(a[8])) {
+      for (int i = 0; i < (pool ? 6 : 5); ++i) written(out[i]);
       Py_INCREF(a[8]);
       return a[8];
     }
@@ -342,6 +352,9 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
           narrow(T, "T"), q ? narrow(q->size(1), "H") : 0, pos, data<int64_t>(sl), plan, &d,
           stream_of(dev));
       if (st != ATTN_OK) return PyLong_FromLong(st);
+      written(tensor(a[2], "k_cache"));
+      written(tensor(a[3], "v_cache"));
+      if (given(a[6])) written(y);
     }
     if (q == nullptr) return Py_NewRef(Py_None);
     return THPVariable_Wrap(std::move(y));
@@ -425,6 +438,9 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
           (m.mask_flags | m.score_flags) != 0 ? &m : nullptr, ws.data_ptr(), (size_t)ws.numel(),
           stream_of(dev));
       if (st != ATTN_OK) return PyLong_FromLong(st);
+      if (given(a[13])) written(out);
+      if (given(a[14])) written(lse);
+      if (given(a[16])) written(ws);
     }
     PyObject* o = THPVariable_Wrap(std::move(out));
     if (!want_lse || o == nullptr) return o;
