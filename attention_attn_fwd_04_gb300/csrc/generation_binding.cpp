@@ -55,6 +55,12 @@ double real(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused();  // such as a tensor of several elements
+  return v != 0;
+}
+
 // dim-dimensional, of this type, on this device, last dimension contiguous
 void rows(const at::Tensor& t, const char* name, at::ScalarType dt, int64_t dim, at::Device dev) {
   if (!t.is_cuda()) refuse("%s must be a CUDA tensor", name);
@@ -145,7 +151,7 @@ bool count(Py_ssize_t n, Py_ssize_t want) {
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count(n, 6)) return nullptr;
   return guarded([&]() -> PyObject* {
-    const bool back = PyObject_IsTrue(a[0]) != 0;
+    const bool back = truth(a[0]);
     const char* name = back ? "dout" : "x";
     const at::Tensor& x = tensor(a[1], name);
     const at::Device dev = x.device();
@@ -390,7 +396,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       flat(s, "alibi_slopes", at::kFloat, {H}, dev);
       m.alibi_slopes = data<float>(s);
     }
-    if (PyObject_IsTrue(a[7]) != 0 || given(a[8])) m.score_flags |= ATTN_SCORE_ALIBI;
+    if (truth(a[7]) || given(a[8])) m.score_flags |= ATTN_SCORE_ALIBI;
     if (given(a[9])) {
       m.softcap = (float)real(a[9]);
       if (m.softcap != 0.0f) m.score_flags |= ATTN_SCORE_SOFTCAP;
@@ -405,7 +411,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const c10::cuda::CUDAGuard guard(dev);
     at::Tensor out, lse, ws;
-    const bool want_lse = PyObject_IsTrue(a[15]) != 0;
+    const bool want_lse = truth(a[15]);
     if (given(a[13])) {
       out = tensor(a[13], "out");
       flat(out, "out", at::kBFloat16, {B, H, D}, dev);
