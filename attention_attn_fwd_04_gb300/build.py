@@ -4,7 +4,8 @@ Each ``csrc/*.cu`` file is compiled in parallel with nvcc
 (``-gencode arch=compute_103a,code=sm_103a``) and the objects are linked into
 one shared library next to this file.  ``csrc/generation_binding.cpp`` becomes
 the CPython module ``_generation`` beside it (host code against PyTorch's and
-Python's headers, linked to the library).  Rebuilds only what changed.
+Python's headers, linked to the library).  Rebuilds only what changed, the
+module also for another PyTorch or Python than it was compiled against.
 
     python -m attention_attn_fwd_04_gb300.build [--force] [--verbose]
 """
@@ -26,7 +27,9 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libattn_gb300.so")
 BINDING_SRC = os.path.join(CSRC, "generation_binding.cpp")
-BINDING = os.path.join(HERE, "_generation.so")
+BINDING = os.path.join(HERE, "_generation" + sysconfig.get_config_var("EXT_SUFFIX"))
+BINDING_OBJ = os.path.join(OBJDIR, "generation_binding.o")
+BINDING_STAMP = os.path.join(OBJDIR, "generation_binding.txt")  # what BINDING was made with
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -74,6 +77,21 @@ def _binding_command(obj: str):
             "-c", BINDING_SRC, "-o", obj]
 
 
+def _binding_made_with() -> str:
+    """What the module depends on beside the repository's files: it holds
+    inlined accessors of one PyTorch's tensors and one Python's objects."""
+    import torch
+    return "\n".join([torch.__version__, sysconfig.get_config_var("SOABI"),
+                      *_binding_command(BINDING_OBJ)])
+
+
+def _binding_stale(hdrs) -> bool:
+    if _stale(BINDING_OBJ, [BINDING_SRC, *hdrs]) or not os.path.exists(BINDING_STAMP):
+        return True
+    with open(BINDING_STAMP) as f:
+        return f.read() != _binding_made_with()
+
+
 def _compile_binding(obj: str) -> str:
     r = subprocess.run(_binding_command(obj), capture_output=True, text=True)
     if r.returncode != 0:
@@ -91,6 +109,12 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, BINDING)
+    # an untagged module, as earlier builds made it, would pass for any Python's
+    untagged = os.path.join(HERE, "_generation.so")
+    if os.path.exists(untagged):
+        os.remove(untagged)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_binding_made_with())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -103,13 +127,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         obj = os.path.join(OBJDIR, os.path.basename(src)[:-3] + ".o")
         if force or _stale(obj, [src, *hdrs]):
             jobs.append((src, obj))
-    bobj = os.path.join(OBJDIR, "generation_binding.o")
-    bind = force or _stale(bobj, [BINDING_SRC, *hdrs])
+    bind = force or _binding_stale(hdrs)
     if jobs or bind:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
             futs = {ex.submit(_compile, s, o, verbose): s for s, o in jobs}
             if bind:
-                futs[ex.submit(_compile_binding, bobj)] = BINDING_SRC
+                futs[ex.submit(_compile_binding, BINDING_OBJ)] = BINDING_SRC
             for f in cf.as_completed(futs):
                 log = f.result()
                 if verbose and log:
@@ -122,8 +145,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s\n%s" % (r.stdout, r.stderr))
         os.replace(tmp, LIB)
-    if bind or _stale(BINDING, [bobj]):
-        _link_binding(bobj)
+    if bind or _stale(BINDING, [BINDING_OBJ]):
+        _link_binding(BINDING_OBJ)
     return LIB
 
 

@@ -306,3 +306,32 @@ def test_native_module_argument_types(attn):
     for fn in (g._native.rope, g._native.slots, g._native.append, g._native.decode):
         with pytest.raises(TypeError):
             fn(x)                                # wrong number of arguments
+
+
+def test_binding_is_rebuilt_for_another_torch_or_python(attn, monkeypatch):
+    # the module inlines accessors of one torch version: a change of torch (or
+    # of the interpreter) has to rebuild it though no source is newer
+    import sysconfig
+
+    from attention_attn_fwd_04_gb300 import build as b
+    from attention_attn_fwd_04_gb300 import _generation
+    assert os.path.samefile(_generation.__file__, b.BINDING)
+    assert b.BINDING.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert not os.path.exists(os.path.join(b.HERE, "_generation.so"))
+    made = []
+    monkeypatch.setattr(b, "_compile_binding", lambda obj: made.append("compiled") or "")
+    monkeypatch.setattr(b, "_link_binding", lambda obj: made.append("linked"))
+    b.build()
+    assert made == []
+    real = sysconfig.get_config_var
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "2.9.1+other")
+        b.build()
+    assert made == ["compiled", "linked"]
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var",
+                  lambda n: "cpython-313-x86_64-linux-gnu" if n == "SOABI" else real(n))
+        b.build()
+    assert made == ["compiled", "linked"] * 2
+    b.build()
+    assert made == ["compiled", "linked"] * 2
