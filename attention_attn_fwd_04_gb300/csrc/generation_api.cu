@@ -423,8 +423,12 @@ attn_status attn_cache_append(const void* q, const int64_t* q_strides, const voi
   // projection's output
   const void* const cp[2] = {cache->k, cache->v};
   const uint64_t cb[2] = {kb, vb};
-  const uint64_t t4 = 4 * (uint64_t)T;
+  const uint64_t t4 = 4 * (uint64_t)T, h4 = 4 * (uint64_t)H_kv;
+  const float* const sc[2] = {cache->k_scale, cache->v_scale};
   for (int i = 0; i < 2; ++i) {
+    if (overlaps(cp[0], cb[0], sc[i], h4) || overlaps(cp[1], cb[1], sc[i], h4) ||
+        overlaps(q_out, 2 * (uint64_t)nqo, sc[i], h4))
+      return ATTN_ERR_INVALID_ARG;
     if (overlaps(cp[i], cb[i], k, 2 * (uint64_t)nk) || overlaps(cp[i], cb[i], v, 2 * (uint64_t)nv) ||
         overlaps(cp[i], cb[i], slots, 2 * t4) || overlaps(cp[i], cb[i], positions, t4) ||
         overlaps(cp[i], cb[i], q, 2 * (uint64_t)nq) ||
@@ -531,13 +535,19 @@ attn_status attn_decode(const void* q, const int64_t* q_strides, const attn_cach
     uint64_t bytes;
   };
   const Part outs[3] = {{out, ob}, {lse, lb}, {workspace, (uint64_t)workspace_bytes}};
-  const Part ins[5] = {{q, 2 * (uint64_t)nq},
+  const bool slopes = (m.score_flags & ATTN_SCORE_ALIBI) != 0u;
+  const bool bias = (m.score_flags & ATTN_SCORE_RELBIAS) != 0u;
+  const Part ins[9] = {{q, 2 * (uint64_t)nq},
                        {cache->k, kb},
                        {cache->v, vb},
                        {block_table, 4 * (uint64_t)nt},
-                       {seq_lens, 4 * (uint64_t)B}};
+                       {seq_lens, 4 * (uint64_t)B},
+                       {cache->k_scale, 4 * (uint64_t)H_kv},
+                       {cache->v_scale, 4 * (uint64_t)H_kv},
+                       {slopes ? m.alibi_slopes : nullptr, 4 * (uint64_t)H},
+                       {bias ? m.rel_bias : nullptr, 4 * (uint64_t)H * (2 * (uint64_t)m.rel_max + 1)}};
   for (int i = 0; i < 3; ++i) {
-    for (int j = 0; j < 5; ++j)
+    for (int j = 0; j < 9; ++j)
       if (overlaps(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return ATTN_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)
       if (overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return ATTN_ERR_INVALID_ARG;

@@ -573,7 +573,8 @@ typedef struct attn_cache_desc {
  *              slot, its elements are left from either of them
  *  plan        the rotation (rot_dim <= D), or NULL: none
  *  cache       where to; E4M3 stores value / scale rounded to nearest even,
- *              values beyond +-448 as +-448, straight from the fp32 result
+ *              values beyond +-448 as +-448, straight from the fp32 result.
+ *              It overlaps no input, its scales among them, and not q_out
  */
 attn_status attn_cache_append(const void *q, const int64_t *q_strides,
                               const void *k, const int64_t *k_strides,
@@ -622,7 +623,8 @@ size_t attn_decode_workspace_bytes(int H, int H_kv, int D);
  *               and LSE = -inf
  *  workspace    device, 16-byte aligned, attn_decode_workspace_bytes():
  *               scratch of this call alone until it has finished, with any
- *               contents
+ *               contents.  out, lse and workspace overlap no input (scales,
+ *               slopes and biases among them) and not one another
  *
  * Pages of a multiple of 16 rows are copied by the TMA, the fast way; any other
  * page size works, row by row.  Waits for copies are bounded by

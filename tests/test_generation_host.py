@@ -214,6 +214,29 @@ def test_decode_cache_refusals(attn, kw, want):
     assert decode_call(attn, d=desc(attn, **kw)) == want
 
 
+def test_outputs_beside_scales_slopes_and_biases(attn):
+    # every array that a call reads while others of its CTAs already write
+    def modded(score_flags, **kw):
+        m = attn.ModDesc()
+        m.version, m.score_flags = 2, score_flags
+        for k, v in kw.items():
+            setattr(m, k, v)
+        return m
+    for out, size in (("out", 2 * 4 * 64 * 2), ("lse", 2 * 4 * 4), ("ws", 1 << 30)):
+        base = dict(out=4 * BIG, lse=7 * BIG, ws=8 * BIG)[out]
+        for at in (base, base + size - 4):
+            for f in ("k_scale", "v_scale"):
+                assert decode_call(attn, d=desc(attn, dtype=1, **{f: at})) == INVALID
+            assert decode_call(attn, mod=modded(attn.SCORE_ALIBI, alibi_slopes=at)) == INVALID
+            assert decode_call(attn, mod=modded(attn.SCORE_RELBIAS, rel_bias=at, rel_max=3)) == INVALID
+        # the last of H (2 R + 1) biases
+        assert decode_call(attn, mod=modded(attn.SCORE_RELBIAS, rel_bias=base - 4 * (4 * 7 - 1),
+                                            rel_max=3)) == INVALID
+    for f in ("k_scale", "v_scale"):
+        for at in (5 * BIG, 6 * BIG + 64, 4 * BIG + 4 * 64 * 2):
+            assert append_call(attn, d=desc(attn, dtype=1, **{f: at})) == INVALID
+
+
 def test_decode_mod_refusals(attn):
     def with_mod(version=2, **kw):
         m = attn.ModDesc()
