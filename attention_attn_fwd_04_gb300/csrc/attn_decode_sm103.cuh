@@ -1355,11 +1355,14 @@ cudaError_t launch_variant(DecodeParams& p, int dev, cudaStream_t stream) {
       warp_grid_of[dev].store(warp_grid, std::memory_order_relaxed);
     }
   }
-  // The most units a row can have, by the table's width and the window.
+  // The most units a row can have, by the table's width and the window: w keys
+  // in a row that begin with a unit's last one reach into (w - 2) / unit + 2.
   const int64_t room = (int64_t)p.a.max_pages * p.a.page_size;
   int64_t most = (room + C::kUnitKeys - 1) / C::kUnitKeys;
-  if (p.a.window > 0 && most > p.a.window / C::kUnitKeys + 2)
-    most = p.a.window / C::kUnitKeys + 2;
+  if (p.a.window > 0) {
+    const int64_t w = ((int64_t)p.a.window + C::kUnitKeys - 2) / C::kUnitKeys + 1;
+    if (most > w) most = w;
+  }
   const int64_t rows = (int64_t)p.a.B * p.a.H_kv * p.runs;
   int cs = 8;
   while (cs > 1 && rows * cs > grid) cs /= 2;
