@@ -36,9 +36,9 @@ Options options_snapshot() {
 // Query tiles per entry of the forward's block masks under these options.
 int mask_tpe(const Options& o) { return o.cta_pair != 0.0 ? kTilesPerQuad : kTilesPerItem; }
 
-// Per-device scratch owned by the library: the status word and the block
-// mask built when the caller passes none.  Allocated on first need, grown
-// when a larger problem arrives, kept until process exit.
+// Per-device scratch owned by the library: the status word's address and the
+// block mask built when the caller passes none.  The mask is allocated on
+// first need, grown when a larger problem arrives, kept until process exit.
 struct DeviceScratch {
   DeviceStatus* status = nullptr;
   void* mask = nullptr;
@@ -51,15 +51,7 @@ attn_status scratch_for(int dev, DeviceScratch** out) {
   std::lock_guard<std::mutex> lk(g_scratch_mu);
   if ((int)g_scratch.size() <= dev) g_scratch.resize(dev + 1);
   DeviceScratch& s = g_scratch[dev];
-  if (s.status == nullptr) {
-    void* p = nullptr;
-    if (cudaMalloc(&p, sizeof(DeviceStatus)) != cudaSuccess) return ATTN_ERR_CUDA;
-    if (cudaMemset(p, 0, sizeof(DeviceStatus)) != cudaSuccess) {
-      cudaFree(p);
-      return ATTN_ERR_CUDA;
-    }
-    s.status = static_cast<DeviceStatus*>(p);
-  }
+  if (s.status == nullptr && status_word_address(&s.status) != cudaSuccess) return ATTN_ERR_CUDA;
   *out = &s;
   return ATTN_OK;
 }
@@ -315,8 +307,8 @@ attn_status load_checked_mod(const attn_mod_desc* in, attn_mod_desc* out) {
 // runs while a stream is being captured into a CUDA graph, runtimes that own
 // all device memory through their own pool or budget, and latency-critical
 // paths that cannot take the device-wide synchronisation cudaMalloc/cudaFree
-// may cause.  attn_fwd allocates its status word and grows its block-mask
-// buffer on first need; attn_fwd_noalloc instead uses this fixed array,
+// may cause.  attn_fwd allocates its block-mask buffer on first need and
+// grows it; attn_fwd_noalloc instead uses this fixed array,
 // which every GPU that loads the library holds until the process exits.
 // Layout: a DeviceStatus in the first kNoAllocStatusBytes, the block mask
 // after it.  Host code must not pass the symbol itself to a kernel (on the

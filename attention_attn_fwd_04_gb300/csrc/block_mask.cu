@@ -23,6 +23,12 @@ namespace attn {
 
 namespace {
 
+// Zero when the library's code is loaded onto a device.  Part of that image
+// and not an allocation, so that a first call can be one under stream
+// capture.  (Here and not beside attn_fwd_noalloc's array, which only its
+// callers should have on their devices.)
+__device__ DeviceStatus g_status_word;
+
 constexpr int kBuildThreads = 256;     // order kernel
 constexpr int kClassifyThreads = 256;   // classify kernel: one key tile per thread
 
@@ -426,6 +432,13 @@ cudaError_t launch_pdl(void (*kern)(Params...), dim3 grid, int threads, cudaStre
 }
 
 }  // namespace
+
+cudaError_t status_word_address(DeviceStatus** out) {
+  void* p = nullptr;
+  const cudaError_t err = cudaGetSymbolAddress(&p, g_status_word);
+  if (err == cudaSuccess) *out = static_cast<DeviceStatus*>(p);
+  return err;
+}
 
 cudaError_t launch_build_block_mask(int B, int S_q, int S_k, const MaskParams& mp,
                                     int force_partial, void* dst, cudaStream_t stream, int tpe) {

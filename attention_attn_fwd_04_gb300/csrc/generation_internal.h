@@ -34,7 +34,7 @@ cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block, 
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
 }
 
-// The current device's status word (allocated on first need).
+// The current device's status word.
 attn_status device_status_word(DeviceStatus** out);
 // The options that bound the kernels' waits.
 void wait_options(double* wait_budget_ms, int* debug_stall);

@@ -234,9 +234,9 @@ attn_status attn_get_device_status(attn_stream_t stream);
  * memory on the call path.
  *
  * No counterpart on the pages this library follows: this entry point exists
- * for callers, not for the method.  attn_fwd allocates a status word and a
- * block-mask buffer on first use (and grows the buffer, with a device-wide
- * synchronisation, when a larger problem arrives).  Callers that cannot do
+ * for callers, not for the method.  attn_fwd allocates a block-mask buffer
+ * on first use (and grows it, with a device-wide synchronisation, when a
+ * larger problem arrives).  Callers that cannot do
  * that -- code running while a stream is captured into a CUDA graph,
  * runtimes that own all device memory through their own pool or budget,
  * latency-critical paths that cannot take the synchronisation of
@@ -370,9 +370,8 @@ attn_status attn_bwd(const void *q, const void *k, const void *v,
  * token-by-token use of a trained model.  Their tensors are bf16 like the
  * rest of the library's and, unlike them, described by strides, in elements:
  * the innermost dimension (D) is always contiguous.  All of them allocate
- * nothing once a device's status word exists (any earlier call on the device,
- * or attn_get_device_status, creates it), keep no state between calls and can
- * be captured in a CUDA graph.  Device-side failures (a page, slot or length
+ * nothing, keep no state between calls and can be captured in a CUDA graph, a
+ * process's first call too.  Device-side failures (a page, slot or length
  * out of range) never touch memory outside the caller's buffers; they are
  * recorded for attn_get_device_status.
  * ------------------------------------------------------------------------- */
