@@ -122,6 +122,14 @@ def rope_plan(rot_dim: int, *, base: float = 10000.0, layout: str = "half",
         raise ValueError("scaling must be one of %s" % sorted(map(str, ROPE_SCALINGS)))
     if mscale is not None and not mscale > 0:
         raise ValueError("mscale must be > 0")
+    # a 0 means the default in the C structure; here it was given
+    read = dict(custom=(), yarn=("base", "beta_fast", "beta_slow"),
+                bands=("base", "low_factor", "high_factor")).get(scaling, ("base",))
+    given = dict(base=base, beta_fast=beta_fast, beta_slow=beta_slow, low_factor=low_factor,
+                 high_factor=high_factor)
+    for name in read:
+        if given[name] == 0:
+            raise ValueError("%s must not be 0" % name)
     c = RopeConfig(version=1, rot_dim=int(rot_dim), layout=ROPE_LAYOUTS[layout],
                    scaling=ROPE_SCALINGS[scaling], base=float(base), factor=float(factor),
                    original_len=float(original_len), beta_fast=float(beta_fast),

@@ -75,6 +75,21 @@ def test_plan_binding_refusals(attn, kw):
         attn.rope_plan(64, **kw)
 
 
+@pytest.mark.parametrize("kw", [
+    dict(base=0.0), dict(base=0, scaling="linear", factor=2.0),
+    dict(scaling="yarn", factor=2.0, original_len=100, beta_fast=0.0),
+    dict(scaling="yarn", factor=2.0, original_len=100, beta_slow=0),
+    dict(scaling="bands", factor=2.0, original_len=100, low_factor=0.0),
+    dict(scaling="bands", factor=2.0, original_len=100, high_factor=0.0)])
+def test_plan_takes_no_zero_for_a_default(attn, kw):
+    # 0 stands for the default in attn_rope_config only
+    with pytest.raises(ValueError):
+        attn.rope_plan(64, **kw)
+    # what a scaling does not read may be anything
+    attn.rope_plan(64, beta_fast=0.0, low_factor=0.0)
+    attn.rope_plan(4, inv_freq=[1.0, 0.5], base=0.0)
+
+
 def arr(*v):
     return (ctypes.c_int64 * len(v))(*v)
 
