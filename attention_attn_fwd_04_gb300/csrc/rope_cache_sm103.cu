@@ -5,7 +5,8 @@
 //   a = p f_i,  (u, v) -> m (u cos a - v sin a, v cos a + u sin a),
 // and its gradient the same with -a.  f_i comes as turns per position in
 // units of 2^-64 (modulo one turn), so p * f_i is an integer product whose
-// low 64 bits are the angle's fraction of a turn, exact for every position;
+// low 64 bits are the angle's fraction of a turn, with no rounding at any
+// position (what is left is p times the plan's own error in f_i, 2^-53 of it);
 // read as a signed number it lies in [-1/2, 1/2) turns.  A product in fp32
 // would be off by 2^-24 p f_i radians: 0.06 at position 2^20 of the fastest
 // pair.  The nearest quarter turn is taken off as an integer too, and sine and

@@ -8,7 +8,9 @@ read and made by a small compiled module (``csrc/generation_binding.cpp``)
 instead of from Python.
 All calls are asynchronous on ``stream`` (default: the current stream of the
 tensors' device).  With ``stream`` given, the tensors a call creates belong to
-that stream.
+that stream.  No call records autograd history: the gradient of :func:`rope`
+is :func:`rope_bwd`, to be called from the caller's own backward pass.  Tensors
+that a call writes into get a new version, as by torch's in-place operations.
 
 A step of a server, with caches seen as ``[num_pages, H_kv, page_size, D]``
 (any strides whose rows are contiguous):
@@ -19,6 +21,15 @@ A step of a server, with caches seen as ``[num_pages, H_kv, page_size, D]``
     q = cache_append(k, v, k_cache, v_cache, m.slots, q=q, plan=plan,
                      positions=m.positions)
     o, lse = attn_decode(q, k_cache, v_cache, table, m.seq_lens)
+
+That is a step in which every request adds one token, so token b is request
+b's.  Where some pause (``new`` 0) or the step is padded to ``max_tokens``, the
+tokens stand closer together than the requests, and the attention takes each
+token's request's row:
+
+    r = m.token_req.clamp(min=0).long()
+    o, lse = attn_decode(q, k_cache, v_cache, table[r],
+                         torch.where(m.token_req >= 0, m.seq_lens[r], 0))
 """
 from __future__ import annotations
 
@@ -181,7 +192,8 @@ def rope(x: torch.Tensor, plan: RopePlan, positions: Optional[torch.Tensor] = No
          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Rotary positions of ``x`` [B, H, S, D] (bf16, any strides with
     contiguous rows): token s of batch b is at ``positions[b, s] + offset``
-    (int32 [S] or [B, S]; default s).  ``out`` may be ``x``."""
+    (int32 [S] or [B, S]; default s).  ``out`` may be ``x``.  The result has no
+    autograd history; :func:`rope_bwd` is the gradient."""
     if stream is not None:
         with _on(stream, x):
             return rope(x, plan, positions, offset=offset, out=out)
@@ -218,8 +230,9 @@ def cache_slots(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: tor
     written into ``block_table`` (int32 [B, max_pages]); without
     ``free_pages`` the table must name them already.  ``out``: tensors of an
     earlier call to write into; its ``seq_lens`` may be ``ctx_lens`` and its
-    ``n_free`` may be ``n_free``.  A step that cannot be served adds nothing
-    and is reported by :func:`get_device_status`."""
+    ``n_free`` may be ``n_free``.  Without it the outputs are parts of one
+    allocation: keeping (or saving) one keeps all.  A step that cannot be
+    served adds nothing and is reported by :func:`get_device_status`."""
     if stream is not None:
         with _on(stream, block_table):
             return cache_slots(ctx_lens, new_lens, block_table, free_pages, n_free,
@@ -279,7 +292,10 @@ def attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     ``block_table`` int32 [B, max_pages], ``seq_lens`` int32 [B] (the newest
     token among them; 0 gives O = 0, LSE = -inf).
     Returns ``(O, LSE)`` (or ``O``), bf16 [B, H, D] and float32 [B, H],
-    written into ``out`` / ``lse`` when given.  Score mods and ``window`` as
+    written into ``out`` / ``lse`` when given, else parts of one allocation
+    (keeping or saving one keeps both).  Short rows are fastest where the table
+    shows that they are: pass the columns of the step's longest request,
+    ``block_table[:, :columns]`` (a view will do).  Score mods and ``window`` as
     for :func:`attn_fwd`; without ``softcap`` a ``rel_bias`` of
     -inf hides its keys.  ``workspace``: uint8 scratch of
     :func:`decode_workspace_bytes` bytes for callers that place it

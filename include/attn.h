@@ -429,8 +429,10 @@ typedef struct attn_rope_config {
 /* A rotation plan: plain host memory, passed to the calls by pointer and
  * read before they return.  turns[i] is pair i's frequency in turns per
  * position, modulo one turn, in units of 2^-64: position * turns[i] modulo
- * 2^64 is the angle at any int32 position, with no rounding that grows
- * with the position. */
+ * 2^64 is the angle at any int32 position, of which the kernels take 32 bits
+ * (1.5e-9 radians).  What the frequency is off by, as the 64-bit float it was
+ * made from (a few steps of 2^-53 of itself), grows with the position like the
+ * angle: 1.3e-7 radians at position 2^31 for a frequency of 1. */
 typedef struct attn_rope_plan {
     uint32_t version;       /* 1                                             */
     int32_t rot_dim;
@@ -605,7 +607,11 @@ size_t attn_decode_workspace_bytes(int H, int H_kv, int D);
  *  block_table  device, int32, row b at b * table_stride; entry t / page_size
  *               names the page of key t; entries of keys that no row sees
  *               are not read.  Rows may share pages
- *  max_pages    columns of the table, max_pages * page_size <= 2^30
+ *  max_pages    columns of the table, max_pages * page_size <= 2^30.  Together
+ *               with the window they bound a row's keys, and calls that can
+ *               only have short rows take shorter ways: pass the columns that
+ *               this step's longest request needs (of a wider table by
+ *               table_stride)
  *  seq_lens     device, int32 [B]: keys of each request, the new token's
  *               among them; 0: O = 0 and LSE = -inf
  *  out          device, bf16 [B][H][D] contiguous, 16-byte aligned
@@ -619,7 +625,7 @@ size_t attn_decode_workspace_bytes(int H, int H_kv, int D);
  *               it does not), a finite one counts as at most 2^127 in
  *               magnitude (a row of biases of the type's lowest value weighs
  *               its keys alike); a row whose keys are all hidden has O = 0
- *               and LSE = -inf
+ *               and LSE = -inf.  ALIBI: slopes times distances below 2^127
  *  workspace    device, 16-byte aligned, attn_decode_workspace_bytes():
  *               scratch of this call alone until it has finished, with any
  *               contents.  out, lse and workspace overlap no input (scales,
@@ -634,7 +640,8 @@ size_t attn_decode_workspace_bytes(int H, int H_kv, int D);
  * A length below 0 or beyond the table counts as the nearest in range, and a
  * page id outside the cache as keys and values of 0; both record
  * ATTN_ERR_DEVICE_CHECK.  Keys and values of rows at and beyond seq_lens[b]
- * may hold anything, infinities and NaN too.
+ * (and before the window) may hold anything, infinities and NaN too.  An infinite
+ * value among those that a row sees makes its column of O NaN.
  */
 attn_status attn_decode(const void *q, const int64_t *q_strides,
                         const attn_cache_desc *cache,
