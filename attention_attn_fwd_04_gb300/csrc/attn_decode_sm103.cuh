@@ -149,7 +149,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMaxBias = 0x1p127f;  // times log2(e) below FLT_MAX
 
 // P of an 8-bit cache is held in fp16, scaled by 2^14: its smallest steps
-// are then 2^-38 of the row's largest weight, beyond what fp32 sums keep.
+// are then 2^-38 of the row's largest weight, beyond what fp32 sums keep of a
+// column to which that weight's value adds.  Where that value is 0 (8-bit
+// values often are) such weights' part of the column is off by up to 2^-39 of
+// their values each.
 constexpr float kHalfShift = 14.0f;
 
 __device__ __forceinline__ void dec_error(DeviceStatus* st, int site, int detail,
