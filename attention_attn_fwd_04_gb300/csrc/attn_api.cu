@@ -11,6 +11,7 @@
 #include <mutex>
 #include <vector>
 
+#include "device_status.h"
 #include "generation_internal.h"
 
 namespace attn {

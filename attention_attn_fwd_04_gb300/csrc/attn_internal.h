@@ -149,9 +149,6 @@ struct DeviceStatus {
   int32_t detail;
 };
 
-// Address of the current device's status word (defined in block_mask.cu).
-cudaError_t status_word_address(DeviceStatus** out);
-
 // Launchers (defined in the .cu files, called by the host API).
 // tpe: query tiles per entry (kTilesPerItem, or kTilesPerQuad for the
 // CTA-pair forward).

@@ -17,6 +17,7 @@
 #include <stdint.h>
 
 #include "attn_internal.h"
+#include "device_status.h"
 #include "sm103_ptx.cuh"
 
 namespace attn {
